@@ -491,6 +491,7 @@ block_sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
         float m_run = ((kMod & kModMask) && ri.mask.x < 0) ? 0.f : -INFINITY;
         float l_run = 0.f;
         bool ok = true;
+        bool started = false;                      // a kept entry has been taken (uniform over the warp)
         for (int e = 0; e < L; ++e) {
             const int b = e & 1;
             const uint32_t s_row = tmem + lane_addr + Cfg::TM_S + 64 * b;
@@ -569,12 +570,16 @@ block_sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                 // kSumLimit.  A row's first kept entry, or a sum above the limit
                 // (or not finite), takes the entry's max instead, raises m (O
                 // rescaled) and writes P again before the hand-off.
-                // (Whole warps take either way, as the TMEM accesses inside are warp-wide.
-                // Without masks a warp's rows have their first kept entry together; with
-                // them a row may wait for its first visible key alone, and the other rows
-                // then take the max of that entry too.)
-                bool slow = (m_run == -INFINITY);
-                if (kMod & kModMask) slow = __any_sync(0xffffffffu, slow && (!hidden || (vis_a | vis_c) != 0u));
+                // (Whole warps take either way, as the TMEM accesses inside are warp-wide, so
+                // the choice must not depend on a row's values: one with a NaN, or with -inf
+                // throughout its first entry, still has m = -inf behind it.  Without masks a
+                // warp's rows have their first kept entry together; with them a row may wait
+                // for its first visible key alone, and the other rows then take the max of
+                // that entry too.)
+                bool slow = !started;
+                started = true;
+                if (kMod & kModMask)
+                    slow = __any_sync(0xffffffffu, m_run == -INFINITY && (!hidden || (vis_a | vis_c) != 0u));
                 if (!slow) {
                     exps((kMod & kModMask) && m_run == -INFINITY ? 0.f : -m_run);
                     slow = !((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]) <= kSumLimit);

@@ -1,0 +1,78 @@
+"""Non-finite values in tokens that are not padding: they stay in the rows they
+belong to, and the calls come back."""
+import pytest
+import torch
+
+from image_dits_b200 import rf2
+from layer_ref import Shape, csr_of, random_kept
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+# 5 and 6 blocks, the last one ragged
+SHAPES = [Shape(1, 2, 64, 5, 8, 7, (1, 8, 8)), Shape(1, 2, 128, 6, 7, 8, (4, 4, 4))]
+# (cap, bias, document mask); None: the unmodified calls
+VARIANTS = [None, (0.0, False, False), (20.0, False, False), (0.0, True, False), (20.0, True, False), (0.0, False, True),
+            (20.0, True, True)]
+
+
+def _mod(sh, variant):
+    if variant is None:
+        return None
+    cap, bias, masked = variant
+    # the last three tokens are padding, the others one document
+    doc = torch.where(torch.arange(sh.n, device=DEV) < sh.n - 3, 4, -1).int()[None].repeat(sh.batch, 1) if masked else None
+    return rf2.ScoreMod(softcap=cap, slopes=torch.full((sh.heads,), 0.2, device=DEV) if bias else None, document=doc)
+
+
+def _qkv(sh, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return [torch.randn((sh.batch, sh.heads, sh.n, sh.dim), generator=g, device=DEV).bfloat16() for _ in range(3)]
+
+
+def _run(sh, q, k, v, mask, mod):
+    lse = torch.empty((sh.batch, sh.heads, sh.n), device=DEV)
+    g = sh.geometry()
+    o = (rf2.block_sparse_attn(g, q, k, v, mask, lse=lse) if mod is None else
+         rf2.block_sparse_attn_mod(g, q, k, v, mask, mod, lse=lse))
+    assert rf2.device_status() == rf2.RF2_OK
+    return o, lse
+
+
+@pytest.mark.parametrize("value", ["nan", "inf", "all -inf"])
+@pytest.mark.parametrize("variant", VARIANTS, ids=str)
+@pytest.mark.parametrize("sh", SHAPES, ids=str)
+def test_forward_of_one_query_row(sh, variant, value):
+    """One row of Q holds a NaN, or an infinity that leaves its first block no finite score: every
+    other row is what it is without, and the row itself is NaN (unless the cap makes an infinite
+    product finite)."""
+    q, k, v = _qkv(sh)
+    mask, mod = csr_of(sh, random_kept(sh, 1.0, 1, DEV)), _mod(sh, variant)
+    k[..., 5] = k[..., 5].abs() + 0.1                     # no zero: an infinity times it is no NaN
+    row = 70
+    bad = q.clone()
+    if value == "nan":
+        bad[0, 1, row, 5] = float("nan")
+    else:
+        bad[0, 1, row, 5] = float("-inf" if value == "all -inf" else "inf")
+        if value == "inf":
+            k[..., :64, 5] *= -1                          # -inf in the first block, +inf behind it
+    want, want_lse = _run(sh, q, k, v, mask, mod)
+    got, got_lse = _run(sh, bad, k, v, mask, mod)
+    others = torch.ones(q.shape[:3], dtype=torch.bool, device=DEV)
+    others[0, 1, row] = False
+    masked, capped = bool(variant and variant[2]), bool(variant and variant[0])
+    if masked or (capped and value != "nan"):
+        # Under a mask such a row may send its warp's rows to their maxima; under the cap an infinite
+        # product moves its warp from one form of tanh to another, each good to 2^-21, so scores of at
+        # most 20 move by 2 * 20 * 2^-21 < 2e-5 and so does the log-sum-exp (less than 10: rounded to
+        # 2^-21 in either run).  The same probabilities to 2e-5, rounded against another maximum (P is
+        # off by 2^-8 of itself each time, O once more).
+        tol = (2 * 2.0 ** -8 + 2e-5) * v.float().abs().max() + 2.0 ** -8 * want.float().abs()
+        assert ((got.float() - want.float()).abs() <= tol)[others].all()
+        if not masked:
+            assert ((got_lse - want_lse).abs() <= 2e-5 + 2.0 ** -20)[others].all()
+    else:
+        assert torch.equal(got[others], want[others]) and torch.equal(got_lse[others], want_lse[others])
+    if value == "nan" or (value == "inf" and not capped):
+        assert torch.isnan(got[0, 1, row]).all()
