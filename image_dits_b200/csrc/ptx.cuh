@@ -443,14 +443,23 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b)
     return *reinterpret_cast<float2*>(&d);
 }
 
+// max(a, b) that gives NaN for a NaN (fmaxf gives the other operand).
+__device__ __forceinline__ float fmax_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // 2^x for x <= ~100 without the special function unit: x = n + r with |r| <= 1/2
 // (n by adding 1.5 * 2^23), 2^r by the minimax polynomial of degree 4 (relative
-// error 2.6e-6, fitted by Remez exchange), n added to the exponent.  x below
-// -126 gives 2^-126: not for values that have to vanish.
+// error 2.6e-6, fitted by Remez exchange), times 2^n put together from its
+// exponent.  x below -126 gives 2^-126: not for values that have to vanish.  A
+// NaN stays one (with n added to the polynomial's exponent bits it would not).
 __device__ __forceinline__ float2 ex2_poly(float2 x)
 {
     const float magic = 12582912.f;
-    x = make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f));
+    x = make_float2(fmax_nan(x.x, -126.f), fmax_nan(x.y, -126.f));
     const float2 t = fadd2(x, make_float2(magic, magic));
     const float2 n = fadd2(t, make_float2(-magic, -magic));
     const float2 r = ffma2(n, make_float2(-1.f, -1.f), x);
@@ -459,8 +468,8 @@ __device__ __forceinline__ float2 ex2_poly(float2 x)
     p = ffma2(r, p, make_float2(0.240247443318367f, 0.240247443318367f));
     p = ffma2(r, p, make_float2(0.6931217908859253f, 0.6931217908859253f));
     p = ffma2(r, p, make_float2(0.9999992847442627f, 0.9999992847442627f));
-    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+    return fmul2(p, make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
+                                __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u)));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)

@@ -76,3 +76,32 @@ def test_forward_of_one_query_row(sh, variant, value):
         assert torch.equal(got[others], want[others]) and torch.equal(got_lse[others], want_lse[others])
     if value == "nan" or (value == "inf" and not capped):
         assert torch.isnan(got[0, 1, row]).all()
+
+
+# three pairs of blocks, each keeping itself and nothing else
+PAIRS = [Shape(1, 2, 64, 6, 8, 8, (1, 8, 8)), Shape(1, 1, 128, 6, 8, 8, (1, 8, 8))]
+
+
+def _pair_mask(sh):
+    kept = torch.zeros((sh.batch * sh.heads, 6, 6), dtype=torch.bool, device=DEV)
+    for p in range(0, 6, 2):
+        kept[:, p:p + 2, p:p + 2] = True
+    return csr_of(sh, kept)
+
+
+@pytest.mark.parametrize("sh", PAIRS, ids=str)
+def test_gradient_keeps_a_query_rows_nan(sh):
+    """A NaN in one row of Q makes its probabilities NaN: all of dV in its pair of blocks, whichever
+    column of the product the row comes to stand in; nothing elsewhere."""
+    q, k, v = _qkv(sh)
+    g, mask = sh.geometry(), _pair_mask(sh)
+    do = torch.randn_like(q)
+    clean = rf2.block_sparse_attn_backward(g, q, k, v, *_run(sh, q, k, v, mask, None), do, mask)
+    for row in range(128, 144):
+        bad = q.clone()
+        bad[:, :, row, 3] = float("nan")
+        got = rf2.block_sparse_attn_backward(g, bad, k, v, *_run(sh, bad, k, v, mask, None), do, mask)
+        assert rf2.device_status() == rf2.RF2_OK
+        assert torch.isnan(got[2][:, :, 128:256]).all(), row
+        for a, b in zip(got, clean):
+            assert torch.equal(a[:, :, :128], b[:, :, :128]) and torch.equal(a[:, :, 256:], b[:, :, 256:])
