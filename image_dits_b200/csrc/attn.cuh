@@ -634,7 +634,9 @@ block_sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             const int qb = qb0 + half;
             const int64_t tok = (int64_t)qb * 64 + (row & 63);
             const bool valid = (qb < Tb) && (tok < args.N);
-            const float inv_l = (l_run > 0.f) ? 1.f / l_run : 0.f;
+            // 0 only where the row has seen no key (or none with a finite score): a NaN stays one
+            const bool none = l_run == 0.f;
+            const float inv_l = none ? 0.f : 1.f / l_run;
             uint16_t* dst = args.op + ((int64_t)bh * args.N + tok) * D;
             #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -659,7 +661,7 @@ block_sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
             }
             if (valid && args.lse) {
                 args.lse[(int64_t)bh * args.N + tok] =
-                    (l_run > 0.f) ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+                    none ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
             }
         }
     }

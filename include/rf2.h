@@ -318,7 +318,8 @@ typedef struct {
 } rf2_score_mod;
 
 /* rf2_block_sparse_attn with modified scores.  A row that sees no key gets
- * an output of 0 and a log-sum-exp of -inf; rows may keep no block.  The output
+ * an output of 0 and a log-sum-exp of -inf; rows may keep no block.  (A NaN
+ * that a row sees makes both NaN.)  The output
  * must not overlap Qp, Kp or Vp (equal pointers are refused).  `workspace`
  * (score_mod_bytes) belongs to the call until it has run: calls that may
  * overlap on the GPU (other streams, graphs replayed side by side) need one

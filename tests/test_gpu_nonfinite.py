@@ -105,3 +105,46 @@ def test_gradient_keeps_a_query_rows_nan(sh):
         assert torch.isnan(got[2][:, :, 128:256]).all(), row
         for a, b in zip(got, clean):
             assert torch.equal(a[:, :, :128], b[:, :, :128]) and torch.equal(a[:, :, 256:], b[:, :, 256:])
+
+
+def _pair_reference(sh, q, k, v, do, softcap):
+    """(O, lse, dQ, dK, dV) in fp64, pair by pair, from the formulas."""
+    outs = []
+    for p in range(3):
+        a, b, c, d = (x[:, :, 128 * p:128 * p + 128].double() for x in (q, k, v, do))
+        s = a @ b.transpose(-1, -2) * sh.dim ** -0.5
+        t = torch.tanh(s / softcap) if softcap else None
+        s = softcap * t if softcap else s
+        m = s.amax(-1, keepdim=True)
+        e = torch.exp(s - m)
+        l = e.sum(-1, keepdim=True)
+        w = e / l
+        o = w @ c
+        ds = w * (d @ c.transpose(-1, -2) - (d * o).sum(-1, keepdim=True)) * (1 - t * t if softcap else 1.0)
+        ds = ds * sh.dim ** -0.5
+        outs.append((o, (m + torch.log(l))[..., 0], ds @ b, ds.transpose(-1, -2) @ a, w.transpose(-1, -2) @ d))
+    return [torch.cat(x, 2) for x in zip(*outs)]
+
+
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("where", ["q", "k", "v", "do"])
+@pytest.mark.parametrize("sh", PAIRS, ids=str)
+def test_nan_reaches_what_it_has_to(sh, where, softcap):
+    """One NaN in a token that sees and is seen: wherever the formulas give NaN the calls do, the
+    log-sum-exp included, and the other pairs of blocks keep their bits."""
+    mask = _pair_mask(sh)
+    mod = rf2.ScoreMod(softcap=softcap) if softcap else None
+    names = ("q", "k", "v", "do")
+    clean = dict(zip(names, (*_qkv(sh), torch.randn((sh.batch, sh.heads, sh.n, sh.dim), device=DEV).bfloat16())))
+    bad = dict(clean)
+    bad[where] = clean[where].clone()
+    bad[where][:, :, 150, 9] = float("nan")
+    outs = []
+    for x in (clean, bad):
+        o, lse = _run(sh, x["q"], x["k"], x["v"], mask, mod)
+        outs.append((o, lse, *rf2.block_sparse_attn_backward(sh.geometry(), x["q"], x["k"], x["v"], o, lse, x["do"], mask, mod)))
+        assert rf2.device_status() == rf2.RF2_OK
+    for name, want, a, b in zip(("o", "lse", "dq", "dk", "dv"), _pair_reference(sh, *(bad[n] for n in names), softcap), *outs):
+        assert torch.isfinite(a.float()).all()
+        assert torch.isnan(b[torch.isnan(want)]).all(), name
+        assert torch.equal(a[:, :, :128], b[:, :, :128]) and torch.equal(a[:, :, 256:], b[:, :, 256:]), name
