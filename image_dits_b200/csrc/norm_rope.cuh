@@ -350,6 +350,21 @@ __global__ void __launch_bounds__(kNormRopeThreads, 2) norm_rope_backward_kernel
                 #pragma unroll
                 for (int q = 0; q < kLoads; ++q) v[q] = ng[q], x[q] = nx[q];
                 if (r0 + kSub < rows) fetch(r0 + kSub);
+                if (norm) {
+                    // A row whose gradient is 0 throughout, as behind the sequence's end and in padding
+                    // tokens, gives 0 and adds nothing to dw, whatever x holds: ones in its place.
+                    auto nonzero = [](const uint4& g) { return ((g.x | g.y | g.z | g.w) & 0x7fff7fffu) != 0u; };
+                    bool all = true;
+                    #pragma unroll
+                    for (int q = 0; q < kLoads; ++q) all = all && nonzero(v[q]);
+                    if (!__all_sync(0xffffffffu, all)) {
+                        const uint32_t lanes = (C == 16 ? 0xffffu : 0xffu) << (rsub * C);
+                        #pragma unroll
+                        for (int q = 0; q < kLoads; ++q)
+                            if (!(__ballot_sync(0xffffffffu, nonzero(v[q])) & lanes))
+                                x[q] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+                    }
+                }
                 #pragma unroll
                 for (int q = 0; q < kLoads; ++q) {
                     const int r = r0 + q * R + rsub;

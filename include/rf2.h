@@ -287,9 +287,9 @@ int rf2_norm_rope_permute(const rf2_geometry* geom, const rf2_norm_rope* params,
  * (read with norm = 1 only), dq, dk (and dv) in token order, and the fp32
  * gradients of the norm weights (device [head_dim] each; each may be NULL;
  * with either, `workspace` holds norm_rope_backward_bytes).  Block means
- * carry no gradient.  Every row enters the weight gradients, one whose
- * gradient is 0 too: its q and k must be finite.  The results do not depend
- * on timing: the sums over tokens and heads run in an order fixed by the
+ * carry no gradient.  A row whose gradient is 0 throughout (a padding token's)
+ * gives 0 and adds nothing to the weight gradients, whatever its q and k
+ * hold.  The results do not depend on timing: the sums over tokens and heads run in an order fixed by the
  * geometry. */
 int rf2_norm_rope_permute_backward(const rf2_geometry* geom, const rf2_norm_rope* params, const rf2_view* q,
                                    const rf2_view* k, const void* dqp, const void* dkp, const void* dvp,
