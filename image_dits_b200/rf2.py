@@ -577,6 +577,13 @@ def _check_mask(geom: Geometry, mask: BlockMask, like: torch.Tensor):
     _same_device(like, mask.row_start, mask.row_count, mask.col_idx)
 
 
+def _check_capacity(geom: Geometry, keep: float, mask: BlockMask):
+    """A prediction at `keep` writes up to that many columns; the kernels know `keep`, not the allocation."""
+    need = query(geom, keep).col_idx_capacity
+    if mask.col_idx.numel() < need:
+        raise ValueError(f"mask: col_idx holds {mask.col_idx.numel()} columns, keep {keep} needs {need}")
+
+
 def _check_lse(geom: Geometry, lse: torch.Tensor, like: torch.Tensor):
     if not (lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()
             and lse.numel() == geom.batch * geom.heads * num_tokens(geom)):
@@ -635,6 +642,7 @@ def predict_mask_visible(geom: Geometry, keep: float, mask: BlockMask, workspace
     """predict_mask_pooled that ranks the key blocks `mod`'s documents and
     order let a query block see before all others.  The block means include
     padding tokens as they are: their Q and K should be finite."""
+    _check_capacity(geom, keep, mask)
     with _On(workspace, stream) as s:
         _scratch(0, workspace, workspace)
         _check_mask(geom, mask, workspace)

@@ -1,0 +1,31 @@
+"""What the binding of the layer operators refuses before any launch, without a GPU."""
+import pytest
+import torch
+
+from image_dits_b200 import build as rf2_build
+from image_dits_b200 import rf2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    rf2_build.build()
+
+
+def geo(**kw):
+    a = dict(batch=2, heads=3, head_dim=128, frames=3, height=7, width=9, win_t=2, win_h=4, win_w=4, sink=True, text=11)
+    a.update(kw)
+    return rf2.make_geometry(**a)
+
+
+@pytest.mark.parametrize("made,used", [(0.2, 0.5), (0.2, 1.0), (0.5, 0.9)])
+def test_visible_prediction_refuses_a_mask_made_for_a_lower_keep(made, used):
+    # host tensors: the refusal comes before anything is looked up on a device
+    g = geo(frames=6, height=16, width=16)
+    mask, ws = rf2.alloc_mask(g, made, "cpu")
+    mod = rf2.ScoreMod(document=torch.zeros((2, rf2.num_tokens(g)), dtype=torch.int32))
+    with pytest.raises(ValueError, match="col_idx"):
+        rf2.predict_mask_visible(g, used, mask, ws, mod)
+    # one made for as much or more gets past it, to the refusal of host tensors
+    for keep in (made, made / 2):
+        with pytest.raises(ValueError, match="CUDA"):
+            rf2.predict_mask_visible(g, keep, mask, ws, mod)
