@@ -420,6 +420,12 @@ def _scratch(nbytes: int, like: torch.Tensor, given: torch.Tensor | None = None)
     return given
 
 
+def _check_three(out, names: str):
+    """Another number of outputs would shift the pointers behind them."""
+    if out is not None and len(out) != 3:
+        raise ValueError(f"out: expected three tensors {names}, got {len(out)}")
+
+
 def _bytes(t: torch.Tensor) -> int:
     return t.numel() * t.element_size()
 
@@ -490,6 +496,7 @@ def norm_rope_permute(geom: Geometry, q, k, v=None, *, q_weight=None, k_weight=N
     with contiguous channels (views of a fused projection, say).  Returns (qp,
     kp, vp), dense; with `workspace` (the mask workspace of alloc_mask) the
     block means are left there as permute_qk_pool does."""
+    _check_three(out, "(qp, kp, vp; None without v)")
     _same_device(q, k, v, q_weight, k_weight, rope and rope.table, workspace)
     with _On(q, stream) as s:
         if workspace is not None:
@@ -517,6 +524,7 @@ def norm_rope_permute_backward(geom: Geometry, q, k, dqp, dkp, dvp=None, *, q_we
     from those of its outputs.  `out`: tensors (dq, dk, dv) to write, of any
     strides (views of a fused projection's gradient, say).  The weight
     gradients are fp32 [d] (None with weight_grads=False or norm=False)."""
+    _check_three(out, "(dq, dk, dv; None without dvp)")
     _same_device(dqp, dkp, dvp, q_weight, k_weight, rope and rope.table, workspace, *((q, k) if norm else ()))
     with _On(dqp, stream) as s:
         _check_qkv(geom, *(t for t in (dqp, dkp, dvp) if t is not None))
@@ -619,6 +627,7 @@ def block_sparse_attn_backward(geom: Geometry, qp, kp, vp, op, lse, dop, mask: B
     """Gradients (dqp, dkp, dvp) of block_sparse_attn (mod None) or
     block_sparse_attn_mod, from its inputs, output and log-sum-exp and the
     output's gradient."""
+    _check_three(out, "(dqp, dkp, dvp)")
     with _On(qp, stream) as s:
         _check_qkv(geom, qp, kp, vp, op, dop)
         if out is None:

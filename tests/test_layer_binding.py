@@ -29,3 +29,24 @@ def test_visible_prediction_refuses_a_mask_made_for_a_lower_keep(made, used):
     for keep in (made, made / 2):
         with pytest.raises(ValueError, match="CUDA"):
             rf2.predict_mask_visible(g, keep, mask, ws, mod)
+
+
+def _bf16(g, n):
+    return [torch.zeros((g.batch, g.heads, rf2.num_tokens(g), g.head_dim), dtype=torch.bfloat16) for _ in range(n)]
+
+
+@pytest.mark.parametrize("n", [0, 1, 2, 4])
+def test_outputs_come_in_threes(n):
+    """Another number of outputs would shift the pointers behind them."""
+    g = geo()
+    x = _bf16(g, 5)
+    out = tuple(_bf16(g, n))
+    mask = rf2.BlockMask(*(torch.zeros(24, dtype=torch.int32) for _ in range(3)), rf2.query(g, 1.0))
+    lse = torch.zeros(2, 3, 200)
+    for call in (lambda: rf2.norm_rope_permute(g, *x[:3], out=out),
+                 lambda: rf2.norm_rope_permute(g, *x[:2], out=out),
+                 lambda: rf2.norm_rope_permute_backward(g, *x, out=out),
+                 lambda: rf2.norm_rope_permute_backward(g, *x[:4], out=out),
+                 lambda: rf2.block_sparse_attn_backward(g, *x[:4], lse, x[4], mask, out=out)):
+        with pytest.raises(ValueError, match="three"):
+            call()
