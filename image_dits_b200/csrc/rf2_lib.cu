@@ -1203,6 +1203,7 @@ int rf2_predict_mask_visible(const rf2_geometry* geom, double keep_ratio, const 
     if (!aligned16(workspace) || !aligned16(row_start) || !aligned16(row_count) || !aligned16(col_idx) ||
         !aligned16(mod_workspace))
         return RF2_ERR_INVALID_ARGUMENT;
+    if (workspace == mod_workspace) return RF2_ERR_INVALID_ARGUMENT;   // the token info would overwrite the means
     const int ms = check_mod(mod);
     if (ms != RF2_OK) return ms;
     if (workspace_bytes < sz.mask_workspace_bytes || mod_workspace_bytes < token_info_bytes(c, geom->batch))

@@ -349,7 +349,8 @@ int rf2_block_sparse_attn_backward(const rf2_geometry* geom, const void* qp_bf16
  * and distance bias do not enter the ranking.  Always selects from the score
  * matrix.  Block means weigh every token of a block, padding included: where
  * blocks mix padding with other tokens, the padding's Q and K should be finite
- * (a NaN there leaves the ranking of its block undefined, not the call). */
+ * (a NaN there leaves the ranking of its block undefined, not the call).
+ * `mod_workspace` (score_mod_bytes) is apart from `workspace`. */
 int rf2_predict_mask_visible(const rf2_geometry* geom, double keep_ratio, const rf2_score_mod* mod,
                              int32_t* row_start, int32_t* row_count, int32_t* col_idx, void* workspace,
                              size_t workspace_bytes, void* mod_workspace, size_t mod_workspace_bytes, void* stream);

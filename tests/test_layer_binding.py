@@ -1,4 +1,6 @@
 """What the binding of the layer operators refuses before any launch, without a GPU."""
+import ctypes
+
 import pytest
 import torch
 
@@ -50,3 +52,16 @@ def test_outputs_come_in_threes(n):
                  lambda: rf2.block_sparse_attn_backward(g, *x[:4], lse, x[4], mask, out=out)):
         with pytest.raises(ValueError, match="three"):
             call()
+
+
+def test_visible_prediction_refuses_one_workspace_for_both():
+    g, a = geo(), 1 << 20
+    m = rf2.ScoreModStruct(0.0, 1.0, 1.0, 1.0, None, None, None)
+    need = rf2.query(g, 0.5).mask_workspace_bytes
+
+    def call(w, mw):
+        # one byte short, so that a call that gets past the pointers stops at the workspace's size
+        return rf2.lib().rf2_predict_mask_visible(ctypes.byref(g), 0.5, ctypes.byref(m), 20 * a, 21 * a, 22 * a, w, need - 1, mw,
+                                                  1 << 30, None)
+    assert call(23 * a, 23 * a) == rf2.RF2_ERR_INVALID_ARGUMENT
+    assert call(23 * a, 24 * a) == rf2.RF2_ERR_INSUFFICIENT_WORKSPACE
