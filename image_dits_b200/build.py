@@ -13,7 +13,7 @@ LIB = os.path.join(HERE, "librf2.so")
 CHECKED_LIB = os.path.join(HERE, "librf2_checked.so")
 SOURCES = ["rf2_lib.cu"]
 DEPS = ["rf2_lib.cu", "attn.cuh", "attn_bwd.cuh", "score_mod.cuh", "norm_rope.cuh", "mask.cuh", "topn.cuh",
-        "permute.cuh", "geometry.cuh", "ptx.cuh"]
+        "permute.cuh", "geometry.cuh", "ptx.cuh", "smem_limits.h"]
 
 
 def nvcc_cmd(out: str, extra=()) -> list:

@@ -11,7 +11,6 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include <mutex>
 
 #include "rf2.h"
 #include "attn.cuh"
@@ -22,6 +21,7 @@
 #include "permute.cuh"
 #include "ptx.cuh"
 #include "score_mod.cuh"
+#include "smem_limits.h"
 #include "topn.cuh"
 
 namespace rf2 {
@@ -185,31 +185,15 @@ static bool current_context_id(unsigned long long* id)
 // raised when a later call needs more.
 static int ensure_dynamic_smem(const void* func, size_t bytes)
 {
-    struct Entry { const void* func; unsigned long long ctx; size_t bytes; };
-    static Entry cache[64];
-    static int used = 0;
-    static std::mutex mu;
+    static SmemLimits limits;
     unsigned long long ctx = 0;
     const bool have_ctx = current_context_id(&ctx);
-    std::lock_guard<std::mutex> lock(mu);
-    Entry* e = nullptr;
-    if (have_ctx)
-        for (int i = 0; i < used; ++i)
-            if (cache[i].func == func && cache[i].ctx == ctx) { e = &cache[i]; break; }
-    if (e && e->bytes >= bytes) return RF2_OK;
-    if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) {
+    const bool ok = limits.ensure(func, have_ctx, ctx, bytes, [](const void* f, size_t n) {
+        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n) == cudaSuccess) return true;
         clear_pending_error();
-        return RF2_ERR_CUDA;
-    }
-    if (!have_ctx) return RF2_OK;
-    if (!e) {
-        e = &cache[used < 64 ? used++ : (int)(ctx % 64)];   // full: overwrite a slot (it is set again when needed)
-        e->func = func;
-        e->ctx = ctx;
-        e->bytes = 0;
-    }
-    e->bytes = bytes;
-    return RF2_OK;
+        return false;
+    });
+    return ok ? RF2_OK : RF2_ERR_CUDA;
 }
 
 static int grid_for_rows(int64_t rows)
