@@ -44,15 +44,18 @@ struct ModArgs {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// tanh from one exponential and one reciprocal: 1 - 2 / (1 + e^(2x)).  Its
-// absolute error stays near 2^-22 (the hardware's tanh.approx has 2^-11,
-// which times a cap of 50 would move scores by 0.02).
-__device__ __forceinline__ float tanh_exp(float x)
+// (tanh x, 1 - tanh^2 x) from one exponential and one reciprocal: with
+// e = e^(-2|x|) and r = 1 / (1 + e), |tanh x| = (1 - e) r and 1 - tanh^2 x =
+// 4 e r^2.  The absolute error of tanh stays near 2^-22 (the hardware's
+// tanh.approx has 2^-11, which times a cap of 50 would move scores by 0.02);
+// the derivative is not formed by subtraction, so its error is relative: a few
+// 1e-6 up to |x| = 10, where 1 - t t of a rounded t has no correct digit.
+__device__ __forceinline__ float2 tanh_exp(float x)
 {
-    const float e = ex2_approx(x * (2.f * kLog2e));
+    const float e = ex2_approx(fabsf(x) * (-2.f * kLog2e));
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
-    return fmaf(-2.f, r, 1.f);
+    return make_float2(copysignf((1.f - e) * r, x), 4.f * e * (r * r));
 }
 
 // tanh(x) = x p(x^2) for |x| <= 1, p the minimax polynomial (relative error
@@ -216,7 +219,8 @@ __device__ __forceinline__ RowInfo load_row_info(const ModArgs& m, int64_t bh, i
 // depends on its largest |x|: up to 1/2, i.e. scores up to half their cap, one
 // of 4 terms in the raw product with every constant factor in its
 // coefficients (5 operations a score); up to 1 the one of 6 terms (9); beyond,
-// the exponential.  Relative error 6e-7 either way.
+// the exponential.  Relative error 6e-7 of the polynomials; absolute 2^-22 of
+// the exponential's tanh.
 template <bool kGrad, int N>
 __device__ __forceinline__ void cap_chunk(uint32_t (&s)[N], uint32_t (&g)[N], const ModArgs& m)
 {
@@ -263,9 +267,9 @@ __device__ __forceinline__ void cap_chunk(uint32_t (&s)[N], uint32_t (&g)[N], co
     } else {
         #pragma unroll
         for (int c = 0; c < N; ++c) {
-            const float t = tanh_exp(__uint_as_float(s[c]) * m.cap_in);
-            s[c] = __float_as_uint(out * t);
-            if (kGrad) g[c] = __float_as_uint(fmaf(-t, t, 1.f));
+            const float2 t = tanh_exp(__uint_as_float(s[c]) * m.cap_in);
+            s[c] = __float_as_uint(out * t.x);
+            if (kGrad) g[c] = __float_as_uint(t.y);
         }
     }
 }
