@@ -41,7 +41,7 @@
 // are bf16, written over the first half of the 32 columns they come from.
 //
 // In the column pass a thread's columns are queries, and their log-sum-exp and
-// delta would be read from shared memory by every thread (2,048 cycles of its
+// delta would be read from shared memory by every thread (1,024 cycles of its
 // 128 bytes a cycle per step, next to the products' own reads).  Instead one
 // more K step of each product subtracts them: the streamed side has -lse
 // sqrt(d) and -delta split into three bf16 each (24 bits), the resident side

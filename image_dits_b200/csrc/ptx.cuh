@@ -453,7 +453,7 @@ __device__ __forceinline__ float fmax_nan(float a, float b)
 
 // 2^x for x <= ~100 without the special function unit: x = n + r with |r| <= 1/2
 // (n by adding 1.5 * 2^23), 2^r by the minimax polynomial of degree 4 (relative
-// error 2.6e-6, fitted by Remez exchange), times 2^n put together from its
+// error below 2.7e-6, fitted by Remez exchange), times 2^n put together from its
 // exponent.  x below -126 gives 2^-126: not for values that have to vanish.  A
 // NaN stays one (with n added to the polynomial's exponent bits it would not).
 __device__ __forceinline__ float2 ex2_poly(float2 x)

@@ -329,8 +329,8 @@ static void mod_args(const Checked& ck, const rf2_geometry* geom, const rf2_scor
     if (!m) return;
     a->cap = m->softcap;
     a->cap_in = m->softcap > 0.f ? (float)(1.0 / (sqrt((double)ck.D) * m->softcap)) : 0.f;
-    // tanh(x) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) for |x| <= 1/2 (relative error 5.4e-7, fitted by Remez
-    // exchange), the factors of x = s cap_in and of the result in the coefficients; a cap far from any
+    // tanh(x) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) for |x| <= 1/2 (relative error below 5.6e-7, 6.2e-7 once
+    // the coefficients are fp32; fitted by Remez exchange), the factors of x = s cap_in and of the result in the coefficients; a cap far from any
     // score would push them out of fp32's range, and keeps to the general polynomial.
     static const double c[4] = {0.999999463558197, -0.33326318860054016, 0.13190296292304993, -0.04440222680568695};
     if (m->softcap > 0.f && m->softcap <= 1e4f) {

@@ -59,7 +59,7 @@ __device__ __forceinline__ float2 tanh_exp(float x)
 }
 
 // tanh(x) = x p(x^2) for |x| <= 1, p the minimax polynomial (relative error
-// 5.9e-7, fitted by Remez exchange); two lanes at a time.  The special
+// below 6.2e-7, fitted by Remez exchange); two lanes at a time.  The special
 // function unit, which gives 4 results per cycle and SM sub-partition, is the
 // scarce one next to a softmax: tanh_exp takes it twice per score, the
 // polynomial leaves it to the exponential.
@@ -219,8 +219,8 @@ __device__ __forceinline__ RowInfo load_row_info(const ModArgs& m, int64_t bh, i
 // depends on its largest |x|: up to 1/2, i.e. scores up to half their cap, one
 // of 4 terms in the raw product with every constant factor in its
 // coefficients (5 operations a score); up to 1 the one of 6 terms (9); beyond,
-// the exponential.  Relative error 6e-7 of the polynomials; absolute 2^-22 of
-// the exponential's tanh.
+// the exponential.  Relative error below 6.2e-7 of the polynomials; absolute
+// 2^-22 of the exponential's tanh.
 template <bool kGrad, int N>
 __device__ __forceinline__ void cap_chunk(uint32_t (&s)[N], uint32_t (&g)[N], const ModArgs& m)
 {
