@@ -146,8 +146,9 @@ struct BwdArgs {
 
 constexpr int kBwdPrepThreads = 256;
 
-// log2 units; of a query without visible keys and of the slots behind the last token: P = 2^(s - 30000) = 0
-constexpr float kDeadLse = 30000.f;
+// log2 units; of a query without visible keys and of the slots behind the last token: P = 2^(s - 1e30) = 0
+// whatever the bias adds to the score (finite, as it goes through the extra K step)
+constexpr float kDeadLse = 1e30f;
 
 // x as the sum of three bf16, two packed words (hi, mid) and (lo, 0).
 __device__ __forceinline__ uint2 split3(float x)

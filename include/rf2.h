@@ -303,6 +303,8 @@ int rf2_norm_rope_permute_backward(const rf2_geometry* geom, const rf2_norm_rope
  *       over the grid positions of the two tokens; 0 where either is a text token
  *   j is visible to i iff its block is kept in the CSR mask, document[i] ==
  *       document[j] >= 0, and order[j] <= order[i]
+ * Scores are fp32: one of size S has the logarithm of its probability off by
+ * about S 2^-23 (a few percent at 2e5).  Slopes may be negative.
  * `document` and `order` are indexed by token in model order (not permuted).
  * Without `document` all tokens share one; without `order` every token sees
  * every other.  Negative documents mark padding: such tokens see nothing and
