@@ -16,9 +16,11 @@
 // 21 x 45 x 80 grid at d = 128) instead of one per token.
 //
 // Both directions move every byte once.  HBM binds the longest calls (720p, 40
-// heads, 4.6 GB in 780 us: 0.91 of a plain copy's rate), instruction issue
-// comes close behind and binds the 480p ones (0.73 forward, 0.70 backward), so
-// what counts is the number of instructions per row.  A CTA takes one 64-token block
+// heads, 4.6 GB in 780 us: 0.91 of a plain copy's rate).  Nothing is saturated
+// in the 480p ones (0.72 forward, 0.69 backward; DRAM at 54% and 53%, issue
+// slots at 58% and 46%): the forward call's last round of CTAs is half empty
+// (1,548 on 444 slots), and the backward kernel has 16 warps an SM at 128
+// registers and stages each item in the open.  A CTA takes one 64-token block
 // of the permuted sequence and up to 24 (head, tensor) units of it: the source
 // rows of the permutation and the (cos, sin) of every token and pair are laid
 // down in shared memory once for all of them (33 KB at d = 128).  A warp takes
@@ -65,7 +67,8 @@ constexpr int kNormRopeThreads = 256;
 // that leaves `waves` rounds of resident CTAs (3 or 2 per SM of 148): few units
 // repeat the staging, few CTAs leave SMs idle in the last round.  Measured:
 // forward, 720p (5,910 CTAs of 24) 780 us, with 8 825; 480p + text (1,548 of
-// 16) 135, with 24 143; backward, 480p 178 with 8, 241 with 24.
+// 16) 135, with 24 143; backward, 480p 178 with 8, 241 with 24 (before the
+// vote on rows without a gradient, which takes 3 us of it).
 constexpr int kNormRopeForwardSlots = 444, kNormRopeForwardWaves = 3;
 constexpr int kNormRopeBackwardSlots = 296, kNormRopeBackwardWaves = 8;
 constexpr int kNormRopeMaxCtas = kNormRopeBackwardSlots;     // backward grid: rows of the partial weight gradients

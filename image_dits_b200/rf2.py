@@ -364,6 +364,8 @@ def rainfusion_attention(geom: Geometry, q, k, v, keep: float, stream=None):
 
 # --------------------------------------------------------------------------
 # The layer around the attention: norms, rotation, score modifications, gradients.
+# The calls record nothing for autograd: what they return has no graph behind it,
+# whatever requires_grad its inputs have; the gradients are the *_backward calls.
 
 
 def layer_query(geom: Geometry) -> LayerSizes:
@@ -688,7 +690,9 @@ def layer_attention(geom: Geometry, q, k, v, keep: float, *, q_weight=None, k_we
     blocks under a document or order mask), block-sparse attention with the
     score modifications, unpermute.  Returns (O, LayerState); the state is what
     layer_attention_backward needs, with the BlockMask in it.  The Q and K of
-    padding tokens (document < 0) should be finite: block means include them."""
+    padding tokens (document < 0) should be finite: block means include them.
+    Like every call here it is not seen by autograd (wrap it and
+    layer_attention_backward in a torch.autograd.Function); norm weights are fp32."""
     params = dict(q_weight=q_weight, k_weight=k_weight, rope=rope, eps=eps, norm=norm, interleaved=interleaved)
     with _On(q, stream) as s:
         mask, ws = alloc_mask(geom, keep, q.device)
