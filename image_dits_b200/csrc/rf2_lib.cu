@@ -11,6 +11,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <new>
 
 #include "rf2.h"
 #include "attn.cuh"
@@ -185,10 +186,11 @@ static bool current_context_id(unsigned long long* id)
 // raised when a later call needs more.
 static int ensure_dynamic_smem(const void* func, size_t bytes)
 {
-    static SmemLimits limits;
+    static SmemLimits* const limits = new (std::nothrow) SmemLimits;   // never destroyed: threads may call until the end
+    if (!limits) return RF2_ERR_CUDA;
     unsigned long long ctx = 0;
     const bool have_ctx = current_context_id(&ctx);
-    const bool ok = limits.ensure(func, have_ctx, ctx, bytes, [](const void* f, size_t n) {
+    const bool ok = limits->ensure(func, have_ctx, ctx, bytes, [](const void* f, size_t n) {
         if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n) == cudaSuccess) return true;
         clear_pending_error();
         return false;
@@ -330,8 +332,9 @@ static void mod_args(const Checked& ck, const rf2_geometry* geom, const rf2_scor
     a->cap = m->softcap;
     a->cap_in = m->softcap > 0.f ? (float)(1.0 / (sqrt((double)ck.D) * m->softcap)) : 0.f;
     // tanh(x) = x (c0 + c1 x^2 + c2 x^4 + c3 x^6) for |x| <= 1/2 (relative error below 5.6e-7, 6.2e-7 once
-    // the coefficients are fp32; fitted by Remez exchange), the factors of x = s cap_in and of the result in the coefficients; a cap far from any
-    // score would push them out of fp32's range, and keeps to the general polynomial.
+    // the coefficients are fp32; fitted by Remez exchange), the factors of x = s cap_in and of the result
+    // in the coefficients; a cap far from any score would push them out of fp32's range, and keeps to the
+    // general polynomial.
     static const double c[4] = {0.999999463558197, -0.33326318860054016, 0.13190296292304993, -0.04440222680568695};
     if (m->softcap > 0.f && m->softcap <= 1e4f) {
         const double in = 1.0 / (sqrt((double)ck.D) * m->softcap), out = 1.4426950408889634 * m->softcap;
